@@ -141,6 +141,7 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 
 // ------------------------------------------------------------ functions
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2eRest = 1.925963033500935e-8f;   // log2 e - kLog2e
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -161,48 +162,127 @@ __device__ __forceinline__ float rcp(float x) {
 }
 __device__ __forceinline__ f2 splat(float x) { return pack2(x, x); }
 
-// 1 / (1 + exp(-x)); where exp(-x) passes the largest float the result is 0.
-__device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
+// Sigmoid and softplus take the type of the plan's activations.  A 16-bit
+// result is rounded to 2^-9 (2^-12) of itself, and an exponential as 2^(x log2 e)
+// with the product rounded once, |x| 2^-24 off, is far below that.  In fp32 it
+// would be the largest error of all, so there exp_minus_2 puts the product's rest
+// back.  Measured over 2^20 points a range, in 2^-24 of the result: sigmoid on
+// [-30, -16], [-16, -7], [-7, -2], [-2, 0] 4.4, 4.0, 3.8, 3.3 at most, rms below 1
+// (with the rounded product 29.9, 15.9, 8.6, 3.6 at most, rms 11.5, 5.7, 2.3, 0.9),
+// between 0 and 20 at most 2.9 either way.  It costs 1 to 2 % of a convolution's,
+// norm's or step's time and 4 to 7 % of a scan's (CUDA's expf and a rounded
+// reciprocal, at most 3.5 off: up to 35 and 19 %).
 
+// exp(-x): with t the rounded x log2 e and r what that rounding left out (log2 e
+// in two parts), 2^-t (1 + r log 2).  Where 2^-t is 0 or infinite it stays so.
+__device__ __forceinline__ f2 exp_minus_2(f2 x) {
+    const f2 t = mul2(x, splat(kLog2e));
+    const f2 r = fma2(x, splat(-kLog2eRest), fma2(x, splat(-kLog2e), t));
+    float t0, t1, e[2], c[2];
+    unpack2(t, t0, t1);
+    e[0] = ex2(-t0);
+    e[1] = ex2(-t1);
+    const f2 raw = pack2(e[0], e[1]);
+    unpack2(fma2(raw, mul2(r, splat(kLn2)), raw), c[0], c[1]);
+    return pack2(fabsf(t0) < 126.f ? c[0] : e[0], fabsf(t1) < 126.f ? c[1] : e[1]);
+}
+
+// 1 / (1 + exp(-x)); where exp(-x) passes the largest float the result is 0.
+template <typename T>
 __device__ __forceinline__ f2 sigmoid_2(f2 x) {
     float a, b;
-    unpack2(add2(ex2_2(mul2(x, splat(-kLog2e))), splat(1.f)), a, b);
+    const f2 e = std::is_same_v<T, float> ? exp_minus_2(x) : ex2_2(mul2(x, splat(-kLog2e)));
+    unpack2(add2(e, splat(1.f)), a, b);
     return pack2(rcp(a), rcp(b));
+}
+template <typename T>
+__device__ __forceinline__ float sigmoid_f(float x) {
+    if constexpr (std::is_same_v<T, float>) {
+        float a, b;
+        unpack2(sigmoid_2<T>(splat(x)), a, b);
+        return a;
+    } else {
+        return rcp(1.f + ex2(x * -kLog2e));
+    }
+}
+
+// Sigmoid s and 1 - s, for the derivatives.  In fp32, 1 - s is exp(-x) s where
+// x > 0: the difference would be off by 2^-24 of 1, and SiLU' by x times that.
+template <typename T>
+__device__ __forceinline__ void sigmoid_and_rest_2(f2 x, f2 &s, f2 &rest) {
+    if constexpr (std::is_same_v<T, float>) {
+        float a, b, x0, x1, r[2], q[2];
+        const f2 e = exp_minus_2(x);
+        unpack2(add2(e, splat(1.f)), a, b);
+        s = pack2(rcp(a), rcp(b));
+        unpack2(fma2(s, splat(-1.f), splat(1.f)), r[0], r[1]);
+        unpack2(mul2(e, s), q[0], q[1]);
+        unpack2(x, x0, x1);
+        rest = pack2(x0 > 0.f ? q[0] : r[0], x1 > 0.f ? q[1] : r[1]);
+    } else {
+        s = sigmoid_2<T>(x);
+        rest = fma2(s, splat(-1.f), splat(1.f));
+    }
 }
 
 // softplus(x) = max(x, 0) + log(1 + e) with e = exp(-|x|) in (0, 1] (an fp32
-// logarithm of 1 + e would lose the small e).  log(1 + e) = e P(e), P fitted
-// to log(1 + e) / e on [0, 1] (Chebyshev points, least squares reweighted
-// towards equal relative errors): 3.0e-8 off at most before rounding, 2.1e-7
-// (rms 5.5e-8) in fp32.
-__device__ __forceinline__ float softplus_f(float x) {
-    const float e = ex2(fabsf(x) * -kLog2e);
-    float p = 0.005232687573879957f;
-    p = fmaf(p, e, -0.02950521931052208f);
-    p = fmaf(p, e, 0.07822593301534653f);
-    p = fmaf(p, e, -0.13663245737552643f);
-    p = fmaf(p, e, 0.19106006622314453f);
-    p = fmaf(p, e, -0.2484298199415207f);
-    p = fmaf(p, e, 0.3331909775733948f);
-    p = fmaf(p, e, -0.4999949336051941f);
-    p = fmaf(p, e, 0.9999999403953552f);
-    return fmaf(p, e, fmaxf(x, 0.f));
+// logarithm of 1 + e would lose the small e).  16-bit plans: log(1 + e) = e P(e),
+// P fitted to log(1 + e) / e on [0, 1] (Chebyshev points, least squares reweighted
+// towards equal relative errors): 3.0e-8 off at most before rounding.  fp32:
+// log(1 + e) = e - e^2 Q(e), Q fitted the same way, 5.1e-9 off at most, so that
+// what is rounded last is small beside e (the whole function within 5 * 2^-24 of
+// itself on [-30, 20]; in 16-bit plans |x| 2^-24 more).  The polynomials take a
+// float or a packed pair.
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+template <typename V, int N>
+__device__ __forceinline__ V horner(const float (&c)[N], V x) {
+    auto as = [](float v) {
+        if constexpr (std::is_same_v<V, f2>) return splat(v);
+        else return v;
+    };
+    V p = as(c[0]);
+#pragma unroll
+    for (int i = 1; i < N; ++i) p = fma2(p, x, as(c[i]));
+    return p;
+}
+template <typename V>
+__device__ __forceinline__ V softplus_p(V e) {
+    const float c[] = {0.005232687573879957f, -0.02950521931052208f, 0.07822593301534653f,
+                       -0.13663245737552643f, 0.19106006622314453f,  -0.2484298199415207f,
+                       0.3331909775733948f,   -0.4999949336051941f,  0.9999999403953552f};
+    return horner(c, e);
+}
+template <typename V>
+__device__ __forceinline__ V softplus_q(V e) {
+    const float c[] = {0.003318469738587737f, -0.02020457200706005f, 0.0576644204556942f,
+                       -0.10680553317070007f, 0.15355394780635834f,  -0.19695399701595306f,
+                       0.24958586692810059f,  -0.33330512046813965f, 0.4999993145465851f};
+    return horner(c, e);
 }
 
+template <typename T>
 __device__ __forceinline__ f2 softplus_2(f2 x) {
     float a, b;
     unpack2(x, a, b);
-    const f2 e = ex2_2(mul2(pack2(fabsf(a), fabsf(b)), splat(-kLog2e)));
-    f2 p = splat(0.005232687573879957f);
-    p = fma2(p, e, splat(-0.02950521931052208f));
-    p = fma2(p, e, splat(0.07822593301534653f));
-    p = fma2(p, e, splat(-0.13663245737552643f));
-    p = fma2(p, e, splat(0.19106006622314453f));
-    p = fma2(p, e, splat(-0.2484298199415207f));
-    p = fma2(p, e, splat(0.3331909775733948f));
-    p = fma2(p, e, splat(-0.4999949336051941f));
-    p = fma2(p, e, splat(0.9999999403953552f));
-    return fma2(p, e, pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+    const f2 linear = pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)), size = pack2(fabsf(a), fabsf(b));
+    if constexpr (std::is_same_v<T, float>) {
+        const f2 e = exp_minus_2(size);
+        return add2(fma2(mul2(e, mul2(e, splat(-1.f))), softplus_q(e), e), linear);
+    } else {
+        const f2 e = ex2_2(mul2(size, splat(-kLog2e)));
+        return fma2(softplus_p(e), e, linear);
+    }
+}
+template <typename T>
+__device__ __forceinline__ float softplus_f(float x) {
+    if constexpr (std::is_same_v<T, float>) {
+        float a, b;
+        unpack2(softplus_2<T>(splat(x)), a, b);
+        return a;
+    } else {
+        const float e = ex2(fabsf(x) * -kLog2e);
+        return fmaf(softplus_p(e), e, fmaxf(x, 0.f));
+    }
 }
 
 // Two neighbouring elements: PAIR, as one access, else as one each (some of

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kConvThreads, WIDE && sizeof(T) == 2 ? 8 : 1) 
 #pragma unroll
                 for (int k = 0; k < K - 2; ++k) win[k][v] = win[k + 1][v];
                 win[K - 2][v] = x;
-                if (p.silu) s = mul2(s, sigmoid_2(s));
+                if (p.silu) s = mul2(s, sigmoid_2<T>(s));
                 out[v] = EDGE && t + j >= len ? 0 : s;
             }
             C::from(out).store(yr + j * yst, left);
@@ -346,8 +346,9 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const __grid_con
                         for (int k = 0; k < K - 1; ++k) pre = fma2(win[k][v], w[k][v], pre);
                         pre = fma2(x, w[K - 1][v], pre);
                         // SiLU'(pre) = s + pre s (1 - s)
-                        const f2 sg = sigmoid_2(pre);
-                        qt = mul2(qt, fma2(mul2(pre, sg), fma2(sg, splat(-1.f), splat(1.f)), sg));
+                        f2 sg, rest;
+                        sigmoid_and_rest_2<T>(pre, sg, rest);
+                        qt = mul2(qt, fma2(mul2(pre, sg), rest, sg));
                     }
                     if (EDGE && tt >= len) qt = 0;
                     const f2 mine = EDGE && tt >= t1 ? 0 : qt;   // tt's term of the weights' gradient is the next run's
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(const __grid_co
     for (int v = 0; v < V / 2; ++v) {
 #pragma unroll
         for (int k = 0; k < K; ++k) s[v] = fma2(h[k].pair(v), w[k][v], s[v]);
-        if (p.silu) s[v] = mul2(s[v], sigmoid_2(s[v]));
+        if (p.silu) s[v] = mul2(s[v], sigmoid_2<T>(s[v]));
     }
     C::from(s).store(yr, left);
     if (to < 0) return;

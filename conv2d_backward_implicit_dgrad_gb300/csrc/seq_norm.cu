@@ -236,8 +236,9 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*red)[32][2], int 
 }
 
 // The gate's factor.
+template <typename T>
 __device__ __forceinline__ float gate_factor(int act, float g) {
-    const float s = sigmoid_f(g);
+    const float s = sigmoid_f<T>(g);
     return act == SEQ_ACT_SILU ? g * s : s;
 }
 
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const __grid_constant__ 
     for (int i = 0; i < E; ++i) b[i] = y[i] * r1 * w[i];
     if (p.gate_act) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) b[i] *= gate_factor(p.gate_act, g[i]);
+        for (int i = 0; i < E; ++i) b[i] *= gate_factor<T>(p.gate_act, g[i]);
     }
     load_param<VEC, E, SHIFT>(p.scale, t, p.tpr, p.channels, p.params_wide, 1.f, w);
     float s[1] = {0.f};
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(MOST, MOST == kPairThreads ? 2 : 512 / MOST) n
                 now.template get<T, 1>(m, w);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const f2 sg = sigmoid_2(w[k]);
+                    const f2 sg = sigmoid_2<T>(w[k]);
                     a[k] = mul2(a[k], silu ? mul2(w[k], sg) : sg);
                 }
             }
@@ -630,8 +631,8 @@ __global__ void __launch_bounds__(MOST, MOST == kPairThreads ? 2 : 512 / MOST) n
                 now.template get<T, 1>(m, g);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const f2 sg = sigmoid_2(g[k]);
-                    const f2 rest = fma2(sg, splat(-1.f), splat(1.f));
+                    f2 sg, rest;
+                    sigmoid_and_rest_2<T>(g[k], sg, rest);
                     const f2 act = silu ? mul2(g[k], sg) : sg;
                     const f2 dact = silu ? fma2(act, rest, sg) : mul2(sg, rest);
                     const f2 db = mul2(dr[k], sc[k]);

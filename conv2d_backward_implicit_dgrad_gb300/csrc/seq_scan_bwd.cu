@@ -269,14 +269,16 @@ __global__ void __launch_bounds__(BwdShape<T, LN, WIDE>::THREADS, BwdShape<T, LN
             const f2 x = add2(v[1], bias[k % S::BIASES]);
             f2 dy = v[2], dz = 0;
             if (p.z.p) {
-                const f2 z = v[3], sz = sigmoid_2(z), zs = mul2(z, sz);
+                f2 sz, rest;
+                sigmoid_and_rest_2<T>(v[3], sz, rest);
+                const f2 zs = mul2(v[3], sz);
                 // SiLU'(z) = s + z s (1 - s)
-                dz = mul2(dy, fma2(zs, fma2(sz, splat(-1.f), splat(1.f)), sz));
+                dz = mul2(dy, fma2(zs, rest, sz));
                 dy = mul2(dy, zs);
             }
             const int i = j * CW + ch;
-            *reinterpret_cast<f2 *>(f_delta + i) = at + j < t1 ? softplus_2(x) : 0;
-            *reinterpret_cast<f2 *>(f_sig + i) = sigmoid_2(x);
+            *reinterpret_cast<f2 *>(f_delta + i) = at + j < t1 ? softplus_2<T>(x) : 0;
+            *reinterpret_cast<f2 *>(f_sig + i) = sigmoid_2<T>(x);
             *reinterpret_cast<f2 *>(f_u + i) = v[0];
             *reinterpret_cast<f2 *>(f_dy + i) = dy;
             *reinterpret_cast<f2 *>(f_dz + i) = dz;

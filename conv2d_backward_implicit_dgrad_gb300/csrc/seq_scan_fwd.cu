@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(scan_threads(LN), scan_blocks(LN, WIDE)) scan_
 #pragma unroll
         for (int jj = 0; jj < kStep; ++jj) {
             const int j = REV ? kStep - 1 - jj : jj;
-            f2 dl = softplus_2(add2(pair_at<T>(cur + (kStep + j) * W::CPB), bias));
+            f2 dl = softplus_2<T>(add2(pair_at<T>(cur + (kStep + j) * W::CPB), bias));
             // behind the last token delta and x are 0 and the state stays
             if (decltype(tail)::value && at + j >= t1) dl = 0;
             sum = add2(sum, dl);
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(scan_threads(LN), scan_blocks(LN, WIDE)) scan_
             if constexpr (REV) {
                 if (p.z.p) {
                     const f2 z = pair_at<T>(cur + (2 * kStep + j) * W::CPB);
-                    x = mul2(x, mul2(z, sigmoid_2(z)));
+                    x = mul2(x, mul2(z, sigmoid_2<T>(z)));
                 }
             } else {
                 x = mul2(x, dl);
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(scan_threads(LN), scan_blocks(LN, WIDE)) scan_
 #pragma unroll
             for (int j = 0; j < kStep; ++j) {
                 const bool in = !decltype(tail)::value || at + j < t1;
-                f2 dl = softplus_2(add2(pair_at<T>(cur + (kStep + j) * W::CPB), bias));
+                f2 dl = softplus_2<T>(add2(pair_at<T>(cur + (kStep + j) * W::CPB), bias));
                 if (decltype(tail)::value && !in) dl = 0;
                 const f2 u = pair_at<T>(cur + j * W::CPB);
                 const f2 x = mul2(u, dl);
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(scan_threads(LN), scan_blocks(LN, WIDE)) scan_
                 }
                 if (p.z.p) {
                     const f2 z = pair_at<T>(cur + (2 * kStep + j) * W::CPB);
-                    y = mul2(y, mul2(z, sigmoid_2(z)));
+                    y = mul2(y, mul2(z, sigmoid_2<T>(z)));
                 }
                 Two<T, WIDE>::store(out + j * ost, 0, in && out0, in && out1, y);
             }
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const __grid_co
         }
         float v[NT];
         load_inputs<T, NT>(static_cast<const T *>(p.B.p) + i * p.B.sb + g * p.B.sg, n0, p.states, p.wide_bc, v);
-        const float dl = softplus_f(dt[r] + bias);
+        const float dl = softplus_f<T>(dt[r] + bias);
         const float x = dl * u[r];
 #pragma unroll
         for (int k = 0; k < NT; ++k) h[r][k] = fmaf(ex2(fmaf(dl, A2[k], kEx2Bias)), h[r][k], x * v[k]);
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(const __grid_co
             }
         }
         if (n0 == 0) {
-            if (p.z.p) y *= z[r] * sigmoid_f(z[r]);
+            if (p.z.p) y *= z[r] * sigmoid_f<T>(z[r]);
             put<T>(outp, 0, y);
         }
     }
