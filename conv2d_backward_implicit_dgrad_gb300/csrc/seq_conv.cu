@@ -322,7 +322,9 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const __grid_con
             }
         }
         // kBwdAhead tokens from t on.  EDGE: some lie behind the row's or the run's
-        // last token, or the grad_x to emit lies before the run.
+        // last token, or the grad_x to emit lies before the run.  Their terms are left
+        // out, not multiplied by 0: an infinite x or weight would make them NaN.
+        const int inner = min(len, t1);
         auto tokens = [&](auto edge, int t) {
             constexpr bool EDGE = decltype(edge)::value;
             C cx[kBwdAhead], cg[kBwdAhead];
@@ -351,14 +353,17 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const __grid_con
                         qt = mul2(qt, fma2(mul2(pre, sg), rest, sg));
                     }
                     if (EDGE && tt >= len) qt = 0;
-                    const f2 mine = EDGE && tt >= t1 ? 0 : qt;   // tt's term of the weights' gradient is the next run's
+                    // tt's term of the weights' gradient; behind the run it is the next run's
+                    if (!EDGE || tt < inner) {
 #pragma unroll
-                    for (int k = 0; k < K - 1; ++k) gw[k][v] = fma2(mine, win[k][v], gw[k][v]);
-                    gw[K - 1][v] = fma2(mine, x, gw[K - 1][v]);
-                    gb[v] = add2(gb[v], mine);
-                    f2 g = mul2(qt, w[0][v]);
+                        for (int k = 0; k < K - 1; ++k) gw[k][v] = fma2(qt, win[k][v], gw[k][v]);
+                        gw[K - 1][v] = fma2(qt, x, gw[K - 1][v]);
+                        gb[v] = add2(gb[v], qt);
+                    }
+                    f2 g = !EDGE || tt < len ? mul2(qt, w[0][v]) : 0;
 #pragma unroll
-                    for (int k = 0; k < K - 1; ++k) g = fma2(q[k][v], w[K - 1 - k][v], g);
+                    for (int k = 0; k < K - 1; ++k)
+                        if (!EDGE || (s + k >= t0 && s + k < len)) g = fma2(q[k][v], w[K - 1 - k][v], g);
                     out[v] = g;
 #pragma unroll
                     for (int k = 0; k < K - 2; ++k) {
@@ -385,7 +390,6 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(const __grid_con
             out_r += kBwdAhead * gst;
         };
         // (grad_final reaches positions len - K + 1 and on, which are emitted at tt >= len: at an edge)
-        const int inner = min(len, t1);
         for (int t = t0; t < te; t += kBwdAhead) {
             if (t >= t0 + K - 1 && t + kBwdAhead <= inner) tokens(std::false_type(), t);
             else tokens(std::true_type(), t);
