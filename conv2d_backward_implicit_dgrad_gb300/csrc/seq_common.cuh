@@ -9,6 +9,7 @@
 #include <atomic>
 #include <cstdint>
 #include <initializer_list>
+#include <numeric>
 #include <type_traits>
 
 #include "dgrad_internal.h"
@@ -398,15 +399,16 @@ inline Span flat(const void *p, size_t bytes) {
                 (long long)bytes};
 }
 
-// Whether two tensors share a byte.  Rows of one buffer side by side (equal
-// distances, columns apart) do not, although their spans do.
+// Whether two tensors may share a byte.  Rows of one buffer side by side (equal
+// distances, columns apart) do not, although their spans do: all of a tensor's
+// rows start a multiple of `pitch` from its first, and columns that keep apart
+// within one pitch keep apart in all.
 inline bool overlaps(const Span &a, const Span &b) {
     if (!a.lo || !b.lo || a.lo >= a.hi || b.lo >= b.hi || a.hi <= b.lo || b.hi <= a.lo) return false;
     if (a.nb == b.nb && a.nt == b.nt && (a.nb == 1 || a.sb == b.sb) && (a.nt == 1 || a.st == b.st)) {
         const long long wa = a.row + (a.ng - 1) * a.sg, wb = b.row + (b.ng - 1) * b.sg;
-        const long long pitch = a.nt > 1 ? a.st : a.sb;
-        const bool regular = a.nt == 1 || a.nb == 1 || (a.st > 0 && a.sb % a.st == 0);
-        if (pitch > 0 && regular) {
+        const long long pitch = std::gcd(a.nb > 1 ? a.sb : 0, a.nt > 1 ? a.st : 0);
+        if (pitch > 0) {
             long long d = (b.lo - a.lo) % pitch;
             if (d < 0) d += pitch;
             // b's columns start d into a's pitch; neither may wrap around into the other
