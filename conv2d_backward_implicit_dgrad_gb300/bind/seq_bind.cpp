@@ -102,6 +102,15 @@ at::Tensor given_or_made(const Spec &s, PyObject *o, const char *name, at::IntAr
     return t ? *t : make(s, shape, type);
 }
 
+// A tensor that the call has written counts as changed in place, so that
+// autograd notices where its backward pass needed the old values.
+void written(const at::Tensor &t) {
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject *o) {
+    if (o != Py_None) written(THPVariable_Unpack(o));
+}
+
 void *stream_of(const Spec &s) {
     return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(s.device)).stream();
 }
@@ -185,6 +194,8 @@ PyObject *conv_run(PyObject *, PyObject *const *a, Py_ssize_t n) {
     q.state = flat<void>(s, given(a[5], "state"), "state", state, s.type);
     q.final_state = flat<void>(s, given(a[7], "final_state"), "final_state", state, s.type);
     settle(seq_conv_run(static_cast<seq_conv_plan_t>(s.plan), &q, stream_of(s)), "seq_conv_run");
+    written(a[6]);
+    written(a[7]);
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }
@@ -217,6 +228,7 @@ PyObject *conv_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     q.grad_bias = bias ? gb.data_ptr<float>() : nullptr;
     q.grad_state = st ? gs.data_ptr() : nullptr;
     settle(seq_conv_backward(static_cast<seq_conv_plan_t>(s.plan), &q, stream_of(s)), "seq_conv_backward");
+    written(a[8]);
     return tuple_of(gx, gw, gb, gs);
     END_HANDLE_TH_ERRORS
 }
@@ -243,6 +255,8 @@ PyObject *conv_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     q.slots = flat<int>(s, given(a[5], "slots"), "slots", {b}, at::kInt);
     q.write_slots = flat<int>(s, given(a[6], "write_slots"), "write_slots", {b}, at::kInt);
     settle(seq_conv_step(static_cast<seq_conv_plan_t>(s.plan), &q, stream_of(s)), "seq_conv_step");
+    written(cache);
+    written(a[7]);
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }
@@ -302,6 +316,9 @@ PyObject *scan_run(PyObject *, PyObject *const *a, Py_ssize_t n) {
     q.final_state = flat(s, given(a[12], "final_state"), "final_state", state);
     q.checkpoints = checkpoints_of(s, given(a[13], "checkpoints"), b, l);
     settle(seq_scan_run(static_cast<seq_scan_plan_t>(s.plan), &q, stream_of(s)), "seq_scan_run");
+    written(a[11]);
+    written(a[12]);
+    written(a[13]);
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }
@@ -350,6 +367,8 @@ PyObject *scan_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     q.grad_dt_bias = bias ? gb.data_ptr<float>() : nullptr;
     q.grad_state = st ? gs.data_ptr<float>() : nullptr;
     settle(seq_scan_backward(static_cast<seq_scan_plan_t>(s.plan), &q, stream_of(s)), "seq_scan_backward");
+    written(a[14]);
+    written(a[15]);
     return tuple_of(gu, gdt, gA, gB, gC, gD, gz, gb, gs);
     END_HANDLE_TH_ERRORS
 }
@@ -381,6 +400,8 @@ PyObject *scan_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
     q.slots = flat<int>(s, given(a[10], "slots"), "slots", {b}, at::kInt);
     q.write_slots = flat<int>(s, given(a[11], "write_slots"), "write_slots", {b}, at::kInt);
     settle(seq_scan_step(static_cast<seq_scan_plan_t>(s.plan), &q, stream_of(s)), "seq_scan_step");
+    written(cache);
+    written(a[12]);
     return wrapped(out);
     END_HANDLE_TH_ERRORS
 }
@@ -414,6 +435,8 @@ PyObject *norm_run(PyObject *, PyObject *const *a, Py_ssize_t n) {
     q.scale = flat(s, given(a[6], "scale"), "scale", {d});
     q.next_weight = flat(s, &needed(a[3], "next_weight"), "next_weight", {d});
     settle(seq_norm_run(static_cast<seq_norm_plan_t>(s.plan), &q, stream_of(s)), "seq_norm_run");
+    written(a[7]);
+    written(a[8]);
     return tuple_of(r, out);
     END_HANDLE_TH_ERRORS
 }
@@ -449,6 +472,9 @@ PyObject *norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     q.grad_scale = scale ? gs.data_ptr<float>() : nullptr;
     q.grad_next_weight = gn.data_ptr<float>();
     settle(seq_norm_backward(static_cast<seq_norm_plan_t>(s.plan), &q, stream_of(s)), "seq_norm_backward");
+    written(a[9]);
+    written(a[10]);
+    written(a[11]);
     return tuple_of(gy, gg, gr, gp, gs, gn);
     END_HANDLE_TH_ERRORS
 }

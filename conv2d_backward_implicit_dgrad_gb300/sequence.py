@@ -16,6 +16,11 @@ strides, channels contiguous).  Sizes in a plan are the largest that its calls
 may bring.  A call allocates the outputs that it is not given.  With an
 explicit ``stream`` (a torch.cuda.Stream) it runs, and allocates, on that
 stream, and the tensors it is given are recorded there.
+
+As with ``Plan``, results carry no autograd graph, whether or not the inputs
+require gradients: training wraps ``run`` and ``backward`` in a
+``torch.autograd.Function`` (``examples/selective_layer.py``).  Tensors that a
+call is given to write (caches, states, outputs) count as changed in place.
 """
 from __future__ import annotations
 
