@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 
 from . import build as _build
 
@@ -107,9 +108,11 @@ def load_library(path: str | None = None):
             if not _build.up_to_date():
                 try:
                     _build.build()
-                except Exception as e:  # no toolchain: fail loudly, never fall back
+                except Exception as e:  # fail loudly, never fall back; an older library (no toolchain here) is named
                     if not os.path.exists(path):
                         raise RuntimeError(f"libdgrad_gb300.so is missing and could not be built: {e}") from e
+                    warnings.warn(f"libdgrad_gb300.so is older than its sources and could not be rebuilt: {e}",
+                                  RuntimeWarning, stacklevel=2)
         lib = ctypes.CDLL(path)
         i, p, vp = ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p
         shape = [i] * 10

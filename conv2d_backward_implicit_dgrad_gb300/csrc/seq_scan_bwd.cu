@@ -40,6 +40,14 @@ namespace {
 
 constexpr int bwd_warps(int ln) { return ln <= 2 ? 2 : 4; }
 
+// A segment of a warp's CW channels in pieces of 16 bytes (8 where it has no more).
+template <typename T, int CW>
+struct BwdPieces {
+    static constexpr int PIECE = (CW * (int)sizeof(T) < 16 ? CW : 16 / (int)sizeof(T));   // elements of one access
+    static constexpr int PIECES = kSeg * CW / PIECE;   // of a warp, segment and tensor
+    static constexpr int COPIES = (PIECES + 31) / 32;  // of a lane
+};
+
 // WIDE: rows lie in 16-byte pieces.
 template <typename T, int LN, bool WIDE>
 struct BwdShape {
@@ -52,9 +60,6 @@ struct BwdShape {
     static constexpr int OWN = LN <= 4 ? 4 / LN : 1;   // channels a lane finishes
     static constexpr int BIASES = CW > 64 ? CW / 64 : 1;  // channel pairs that a lane prepares
     static constexpr int ITEMS = CW >= 8 ? CW / 8 : 1; // (token, channel pair)s a lane prepares of a segment
-    static constexpr int PIECE = (CW * (int)sizeof(T) < 16 ? CW : 16 / (int)sizeof(T));   // elements of one access
-    static constexpr int PIECES = kSeg * CW / PIECE;   // of a warp, segment and tensor
-    static constexpr int COPIES = (PIECES + 31) / 32;  // of a lane
     static constexpr int BCS = (kSeg * 2 * NP + THREADS - 1) / THREADS;   // elements of B and C a thread loads
     // shared memory, in floats
     static constexpr int STATE = 32 * 16;              // a warp's states
@@ -92,6 +97,7 @@ __global__ void __launch_bounds__(BwdShape<T, LN, WIDE>::THREADS, BwdShape<T, LN
     scan_bwd_kernel(const __grid_constant__ ScanParams p) {
     begin_kernel();
     using S = BwdShape<T, LN, WIDE>;
+    using Q = BwdPieces<T, S::CW>;
     constexpr int NP = S::NP, CW = S::CW, OWN = S::OWN, LD = S::LD;
     extern __shared__ __align__(16) float sm[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -192,16 +198,16 @@ __global__ void __launch_bounds__(BwdShape<T, LN, WIDE>::THREADS, BwdShape<T, LN
     auto load_ahead = [&](int at) {
         if constexpr (WIDE) {
 #pragma unroll
-            for (int k = 0; k < S::COPIES; ++k) {
+            for (int k = 0; k < Q::COPIES; ++k) {
                 const int e = lane + 32 * k;
-                const int j = e / (CW / S::PIECE), c = e % (CW / S::PIECE) * S::PIECE;
-                if (S::PIECES % 32 != 0 && j >= kSeg) continue;
+                const int j = e / (CW / Q::PIECE), c = e % (CW / Q::PIECE) * Q::PIECE;
+                if (Q::PIECES % 32 != 0 && j >= kSeg) continue;
                 const bool on = at + j < t1 && c < left;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const T *const from = scan_row<T>(*in[i], b, at) + (dbase + j * token_step(*in[i]) + c);
                     const bool there = on && (i < 3 || p.z.p);
-                    copy_ahead<S::PIECE * sizeof(T)>(raw + (i * kSeg + j) * CW + c, there ? from : static_cast<const T *>(p.u.p), there);
+                    copy_ahead<Q::PIECE * sizeof(T)>(raw + (i * kSeg + j) * CW + c, there ? from : static_cast<const T *>(p.u.p), there);
                 }
             }
         } else {
@@ -432,17 +438,17 @@ __global__ void __launch_bounds__(BwdShape<T, LN, WIDE>::THREADS, BwdShape<T, LN
             T *const row = scan_row<T>(o, b, at) + dbase;
             if constexpr (WIDE) {
 #pragma unroll
-                for (int k = 0; k < S::COPIES; ++k) {
+                for (int k = 0; k < Q::COPIES; ++k) {
                     const int e = lane + 32 * k;
-                    const int j = e / (CW / S::PIECE), c = e % (CW / S::PIECE) * S::PIECE;
+                    const int j = e / (CW / Q::PIECE), c = e % (CW / Q::PIECE) * Q::PIECE;
                     if (j >= kSeg || at + j >= t1 || c >= left) continue;
-                    float v[S::PIECE];
+                    float v[Q::PIECE];
 #pragma unroll
-                    for (int m = 0; m < S::PIECE; m += 4) {
+                    for (int m = 0; m < Q::PIECE; m += 4) {
                         const float4 q = *reinterpret_cast<const float4 *>(f + j * CW + c + m);
                         v[m] = q.x; v[m + 1] = q.y; v[m + 2] = q.z; v[m + 3] = q.w;
                     }
-                    *reinterpret_cast<Vec<T, S::PIECE> *>(row + (j * token_step(o) + c)) = Vec<T, S::PIECE>::from(v);
+                    *reinterpret_cast<Vec<T, Q::PIECE> *>(row + (j * token_step(o) + c)) = Vec<T, Q::PIECE>::from(v);
                 }
             } else {
                 for (int e = lane; e < S::FIELD; e += 32) {

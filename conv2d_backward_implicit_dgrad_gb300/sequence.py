@@ -27,6 +27,7 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
+import warnings
 from collections import namedtuple
 
 from . import build as _build
@@ -54,6 +55,15 @@ def _library():
     if _LIB is None:
         import torch  # noqa: F401 (the call module links against it)
         lib = load_library()
+        if not _build.bind_up_to_date():
+            try:
+                _build.build_bind()
+            except Exception as e:
+                if not _build.bind_fits():
+                    raise RuntimeError("the sequence operators' call module is missing, or was built for another "
+                                       f"PyTorch or Python, and could not be built: {e}") from e
+                warnings.warn(f"{_build.BIND} is older than its source and could not be rebuilt: {e}", RuntimeWarning,
+                              stacklevel=2)
         i, q, vp, f = ctypes.c_int, ctypes.c_longlong, ctypes.c_void_p, ctypes.c_float
         lib.seq_conv_plan.argtypes = [q, q, q, i, i, i, ctypes.POINTER(vp)]
         lib.seq_scan_plan.argtypes = [q, q, q, i, i, i, ctypes.POINTER(vp)]
