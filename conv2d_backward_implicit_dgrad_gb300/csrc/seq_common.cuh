@@ -376,6 +376,7 @@ struct PlanBase {
     int device, sm_count;
     uint32_t *err;   // device word: 1 after a slot out of range
 };
+constexpr size_t kErrorBytes = 256;   // that err points to
 
 inline size_t elem_size(seq_dtype_t d) { return d == SEQ_F32 ? 4 : 2; }
 

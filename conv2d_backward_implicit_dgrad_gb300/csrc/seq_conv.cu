@@ -580,6 +580,10 @@ size_t most_parts(const seq_conv_plan_s *pl) {
     return (size_t)std::max(full, some);
 }
 
+size_t conv_bwd_need(const seq_conv_plan_s *pl) {
+    return most_parts(pl) * (size_t)pl->channels * (pl->width + 1) * 4;
+}
+
 bool conv_wide(const seq_conv_plan_s *pl, ConvOp op, std::initializer_list<const seq_ref_t *> refs,
                std::initializer_list<const void *> flats) {
     const size_t es = elem_size(pl->dtype);
@@ -691,7 +695,7 @@ dgrad_status_t seq_conv_backward(seq_conv_plan_t pl, const seq_conv_grad_args_t 
     const bool wide = conv_wide(pl, kBwd, {&a->x, &a->grad_y, &a->grad_x}, {a->state, a->grad_state, a->grad_final});
     const int v = wide ? wide_channels(kBwd) : 2;
     const ConvShape c = conv_shape(pl, a->batch, a->length, v);
-    if ((st = grow(&pl->part, &pl->part_bytes, most_parts(pl) * D * (K + 1) * 4)) != DGRAD_OK) return st;
+    if ((st = grow(&pl->part, &pl->part_bytes, conv_bwd_need(pl))) != DGRAD_OK) return st;
     ConvParams p{};
     p.batch = a->batch;
     p.length = a->length;
@@ -760,6 +764,10 @@ dgrad_status_t seq_conv_step(seq_conv_plan_t pl, const seq_conv_step_args_t *a, 
 }
 
 dgrad_status_t seq_conv_check(seq_conv_plan_t pl) { return pl ? read_error(pl->base) : DGRAD_ERR_INVALID_ARG; }
+
+size_t seq_conv_workspace_bytes(seq_conv_plan_t pl, int gradients) {
+    return pl ? kErrorBytes + (gradients ? conv_bwd_need(pl) : 0) : 0;
+}
 
 void seq_conv_destroy(seq_conv_plan_t pl) {
     if (!pl) return;

@@ -887,6 +887,14 @@ int norm_bwd_grid(const seq_norm_plan_s *pl, long long rows, const NormShape &s,
     return (int)std::min(fill, (rows + per_block - 1) / per_block);
 }
 
+// Partial rows of any call of the plan.
+size_t norm_bwd_need(const seq_norm_plan_s *pl) {
+    int blocks = 0;
+    for (const bool w : {false, true})
+        blocks = std::max(blocks, norm_bwd_grid(pl, pl->rows, norm_shape(pl->channels, bwd_elems(pl->channels, w)), w));
+    return (size_t)blocks * 3 * pl->channels * 4;
+}
+
 bool norm_refs_wide(const seq_norm_plan_s *pl, std::initializer_list<const seq_ref_t *> acts,
                     std::initializer_list<const seq_ref_t *> residuals, std::initializer_list<const float *> params) {
     const size_t es = elem_size(pl->dtype), rs = elem_size(pl->rtype);
@@ -1012,11 +1020,7 @@ dgrad_status_t seq_norm_backward(seq_norm_plan_t pl, const seq_norm_grad_args_t 
                                      {&a->residual, &a->grad_residual_out, &a->grad_residual},
                                      {a->post_weight, a->scale, a->next_weight});
     const NormShape sh = norm_shape(pl->channels, bwd_elems(pl->channels, wide));
-    int blocks = 0;   // of any call of the plan
-    for (const bool w : {false, true})
-        blocks = std::max(blocks, norm_bwd_grid(pl, pl->rows, norm_shape(pl->channels, bwd_elems(pl->channels, w)), w));
-    const size_t most = (size_t)blocks * 3 * D * 4;
-    if ((st = grow(&pl->part, &pl->part_bytes, most)) != DGRAD_OK) return st;
+    if ((st = grow(&pl->part, &pl->part_bytes, norm_bwd_need(pl))) != DGRAD_OK) return st;
     NormParams p{};
     fill_norm(pl, sh, &p);
     p.rows = n;
@@ -1043,6 +1047,10 @@ dgrad_status_t seq_norm_backward(seq_norm_plan_t pl, const seq_norm_grad_args_t 
     const int sums = p.n_part * (int)D;
     return dgrad::cuda_status(launch(norm_grad_sum_kernel, (sums + 31) / 32, 32 * kSumWarps, 0, s, p.part, grid, sums, (int)D,
                                      a->grad_next_weight, g1, g2));
+}
+
+size_t seq_norm_workspace_bytes(seq_norm_plan_t pl, int gradients) {
+    return pl ? kErrorBytes + (gradients ? norm_bwd_need(pl) : 0) : 0;
 }
 
 void seq_norm_destroy(seq_norm_plan_t pl) {

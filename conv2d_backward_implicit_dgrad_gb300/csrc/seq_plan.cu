@@ -19,11 +19,11 @@ dgrad_status_t open_plan(PlanBase *base) {
     base->device = dev;
     base->err = nullptr;
     void *mem = nullptr;
-    if (cudaMalloc(&mem, 256) != cudaSuccess) {
+    if (cudaMalloc(&mem, kErrorBytes) != cudaSuccess) {
         cudaGetLastError();
         return DGRAD_ERR_OOM;
     }
-    if (cudaMemset(mem, 0, 256) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
+    if (cudaMemset(mem, 0, kErrorBytes) != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) {
         cudaGetLastError();
         cudaFree(mem);
         return DGRAD_ERR_CUDA;

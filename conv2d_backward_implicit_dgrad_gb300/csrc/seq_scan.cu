@@ -340,6 +340,10 @@ dgrad_status_t seq_scan_step(seq_scan_plan_t pl, const seq_scan_step_args_t *a, 
 
 dgrad_status_t seq_scan_check(seq_scan_plan_t pl) { return pl ? read_error(pl->base) : DGRAD_ERR_INVALID_ARG; }
 
+size_t seq_scan_workspace_bytes(seq_scan_plan_t pl, int gradients) {
+    return pl ? kErrorBytes + fwd_need(pl) + (gradients ? bwd_need(pl) : 0) : 0;
+}
+
 void seq_scan_destroy(seq_scan_plan_t pl) {
     if (!pl) return;
     void *mems[] = {pl->fwd, pl->bwd};

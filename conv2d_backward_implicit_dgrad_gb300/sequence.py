@@ -13,7 +13,9 @@ in ``bind/seq_bind.cpp`` (a Python module of its own: for single tokens the
 checks in Python would take longer than the kernels).  Activations are
 token-major, channels innermost; rows may be slices of wider tensors (any
 strides, channels contiguous).  Sizes in a plan are the largest that its calls
-may bring.  A call allocates the outputs that it is not given.  With an
+may bring, and size its workspace: device memory of its own, outside PyTorch's
+allocator (``workspace_bytes``; the gradients' share is taken by the first
+``backward``, after ``torch.cuda.empty_cache`` where there is no room).  A call allocates the outputs that it is not given.  With an
 explicit ``stream`` (a torch.cuda.Stream) it runs, and allocates, on that
 stream, and the tensors it is given are recorded there.
 
@@ -34,13 +36,15 @@ from . import build as _build
 from .binding import DgradError, load_library
 
 DTYPE = {"fp32": 0, "fp16": 1, "bf16": 2}
+OUT_OF_MEMORY = 5   # DGRAD_ERR_OOM
 ACT = {"none": 0, "silu": 1, "sigmoid": 2}
 
 # Every function declared in include/seq.h (checked by the CPU tests).
 SEQ_EXPORTS = ("seq_conv_plan", "seq_conv_run", "seq_conv_backward", "seq_conv_step", "seq_conv_check",
-               "seq_conv_destroy", "seq_scan_plan", "seq_scan_checkpoint_bytes", "seq_scan_run",
-               "seq_scan_backward", "seq_scan_step", "seq_scan_check", "seq_scan_destroy", "seq_norm_plan",
-               "seq_norm_run", "seq_norm_backward", "seq_norm_destroy")
+               "seq_conv_workspace_bytes", "seq_conv_destroy", "seq_scan_plan", "seq_scan_checkpoint_bytes",
+               "seq_scan_run", "seq_scan_backward", "seq_scan_step", "seq_scan_check", "seq_scan_workspace_bytes",
+               "seq_scan_destroy", "seq_norm_plan", "seq_norm_run", "seq_norm_backward", "seq_norm_workspace_bytes",
+               "seq_norm_destroy")
 
 ConvGrads = namedtuple("ConvGrads", "x weight bias state")
 ScanGrads = namedtuple("ScanGrads", "u dt A B C D z dt_bias state")
@@ -72,6 +76,8 @@ def _library():
             getattr(lib, name + "_plan").restype = i
             getattr(lib, name + "_destroy").argtypes = [vp]
             getattr(lib, name + "_destroy").restype = None
+            getattr(lib, name + "_workspace_bytes").argtypes = [vp, i]
+            getattr(lib, name + "_workspace_bytes").restype = ctypes.c_size_t
             if name != "seq_norm":
                 getattr(lib, name + "_check").argtypes = [vp]
                 getattr(lib, name + "_check").restype = i
@@ -95,9 +101,13 @@ class _SeqPlan:
         self._lib = _library()
         self._h = ctypes.c_void_p()
         self.dtype = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}[dtype]
-        st = getattr(self._lib, f"seq_{self._kind}_plan")(*args, ctypes.byref(self._h))
-        if st != 0:
-            raise DgradError(st, f"seq_{self._kind}_plan")
+
+        def make():
+            st = getattr(self._lib, f"seq_{self._kind}_plan")(*args, ctypes.byref(self._h))
+            if st != 0:
+                raise DgradError(st, f"seq_{self._kind}_plan")
+
+        self._with_room(make)
         self.device = torch.cuda.current_device()
         self._c = _BIND.open_plan(self._h.value, self.device, DTYPE[dtype], DTYPE[residual or dtype], batch, length,
                                   channels, inner, groups, gated)
@@ -105,6 +115,27 @@ class _SeqPlan:
     def _alive(self):
         if not self._h:
             raise ValueError("the plan is closed")
+
+    def _with_room(self, call, *args):
+        """The call; where the plan's workspace found no memory, once more after PyTorch has given back what it holds
+        unused."""
+        try:
+            return call(*args)
+        except DgradError as e:
+            if e.status != OUT_OF_MEMORY:
+                raise
+        self._torch.cuda.empty_cache()
+        return call(*args)
+
+    def _backward(self, call, args, stream):
+        if stream is not None:
+            return self._with_room(self._on, stream, call, *args)
+        return self._with_room(call, self._c, *args)
+
+    def workspace_bytes(self, gradients=True):
+        """Device memory that the plan holds for itself, without or with backward calls."""
+        self._alive()
+        return getattr(self._lib, f"seq_{self._kind}_workspace_bytes")(self._h, int(bool(gradients)))
 
     def _on(self, stream, call, *args):
         """The call on an explicit stream, which is told which tensors it uses."""
@@ -172,9 +203,7 @@ class CausalConvPlan(_SeqPlan):
     def backward(self, grad_out, x, weight, bias=None, lengths=None, state=None, grad_final_state=None, grad_x=None,
                  stream=None):
         args = (grad_out, x, weight, bias, lengths, state, grad_final_state, grad_x)
-        if stream is not None:
-            return ConvGrads._make(self._on(stream, _BIND.conv_backward, *args))
-        return ConvGrads._make(_BIND.conv_backward(self._c, *args))
+        return ConvGrads._make(self._backward(_BIND.conv_backward, args, stream))
 
     def step(self, x, weight, cache, bias=None, slots=None, write_slots=None, out=None, stream=None):
         if stream is not None:
@@ -223,9 +252,7 @@ class ScanPlan(_SeqPlan):
     def backward(self, grad_out, u, dt, A, B, C, checkpoints, D=None, z=None, dt_bias=None, lengths=None, state=None,
                  grad_final_state=None, grad_u=None, grad_z=None, stream=None):
         args = (grad_out, u, dt, A, B, C, checkpoints, D, z, dt_bias, lengths, state, grad_final_state, grad_u, grad_z)
-        if stream is not None:
-            return ScanGrads._make(self._on(stream, _BIND.scan_backward, *args))
-        return ScanGrads._make(_BIND.scan_backward(self._c, *args))
+        return ScanGrads._make(self._backward(_BIND.scan_backward, args, stream))
 
     def step(self, u, dt, A, B, C, cache, D=None, z=None, dt_bias=None, slots=None, write_slots=None, out=None,
              stream=None):
@@ -274,6 +301,4 @@ class BlockNormPlan(_SeqPlan):
                  grad_y=None, grad_gate=None, grad_residual=None, stream=None):
         args = (grad_residual_out, grad_out, y, residual, next_weight, post_weight, gate, scale, grad_y, grad_gate,
                 grad_residual)
-        if stream is not None:
-            return NormGrads._make(self._on(stream, _BIND.norm_backward, *args))
-        return NormGrads._make(_BIND.norm_backward(self._c, *args))
+        return NormGrads._make(self._backward(_BIND.norm_backward, args, stream))

@@ -21,7 +21,11 @@
  * The first backward call of a plan allocates its share of the workspace (so
  * make one before capturing a graph); nothing else allocates.  A plan's
  * batch, length and rows are the largest that its calls may bring; each call
- * gives its own.  Outputs are fully overwritten; an output that overlaps an
+ * gives its own.  The workspace is sized for the largest, by cudaMalloc, and
+ * kept until the plan is destroyed; seq_*_workspace_bytes() says how much that
+ * is without (gradients 0) and with backward calls (1), and each operator's
+ * part below what it grows with.  Where there is no room the call returns
+ * DGRAD_ERR_OOM, has launched nothing and can be made again.  Outputs are fully overwritten; an output that overlaps an
  * input returns DGRAD_ERR_ALIAS (interleaved slices of one buffer do not
  * overlap), a pointer that is not a multiple of its element size
  * DGRAD_ERR_MISALIGNED (16-byte alignment and strides are faster, and not
@@ -73,7 +77,8 @@ typedef struct {
  * with x before the first token taken from `state` ([batch, K-1, channels],
  * oldest first, contiguous; NULL: zeros).  final_state receives the last K-1
  * inputs of each row (earlier state rows among them where the row is shorter).
- * K is 2, 3 or 4. */
+ * K is 2, 3 or 4.  Workspace with gradients: 4 (K + 1) channels P bytes, P the
+ * larger of batch ceil(length / 256) and 768 SMs / ceil(channels / 4) + 1 + batch. */
 typedef struct seq_conv_plan_s *seq_conv_plan_t;
 
 typedef struct {
@@ -118,6 +123,7 @@ dgrad_status_t seq_conv_run(seq_conv_plan_t plan, const seq_conv_args_t *args, v
 dgrad_status_t seq_conv_backward(seq_conv_plan_t plan, const seq_conv_grad_args_t *args, void *stream);
 dgrad_status_t seq_conv_step(seq_conv_plan_t plan, const seq_conv_step_args_t *args, void *stream);
 dgrad_status_t seq_conv_check(seq_conv_plan_t plan);
+size_t seq_conv_workspace_bytes(seq_conv_plan_t plan, int gradients);
 void seq_conv_destroy(seq_conv_plan_t plan);
 
 /* ------------------------------------------------------------------ seq_scan
@@ -130,7 +136,16 @@ void seq_conv_destroy(seq_conv_plan_t plan);
  * states] fp32, contiguous (state NULL: zeros).
  *
  * checkpoints (training): seq_scan_checkpoint_bytes() bytes that the run
- * fills with the states at every 8th token and the backward call reads. */
+ * fills with the states at every 8th token and the backward call reads.
+ *
+ * Workspace, with C = min(64, length / 16) chunks and P the channels, each
+ * group's rounded up to a multiple of 4: 4 batch C P (states + 1) bytes (none
+ * where C is 1 or less).  Gradients add 4 batch C P (states + 2) and, for the
+ * parts of grad_B and grad_C, 32 q T batch length groups bytes: q is states / 4
+ * rounded up to a power of two, T the column tiles of a group, of 256, 128, 128,
+ * 64, 32, 16 channels for q = 1, 2, 4, 8, 16, 32.  Those parts grow with states
+ * times channels: 1 KB a token and group at 16 states and 1024 channels, 131 KB
+ * at 64 states and 8192 channels, 524 KB at 128. */
 typedef struct seq_scan_plan_s *seq_scan_plan_t;
 
 typedef struct {
@@ -173,6 +188,7 @@ dgrad_status_t seq_scan_run(seq_scan_plan_t plan, const seq_scan_args_t *args, v
 dgrad_status_t seq_scan_backward(seq_scan_plan_t plan, const seq_scan_grad_args_t *args, void *stream);
 dgrad_status_t seq_scan_step(seq_scan_plan_t plan, const seq_scan_step_args_t *args, void *stream);
 dgrad_status_t seq_scan_check(seq_scan_plan_t plan);
+size_t seq_scan_workspace_bytes(seq_scan_plan_t plan, int gradients);
 void seq_scan_destroy(seq_scan_plan_t plan);
 
 /* ------------------------------------------------------------------ seq_norm
@@ -184,7 +200,8 @@ void seq_scan_destroy(seq_scan_plan_t plan);
  * residual scale, the residual add and the norm before the next block.  r' is
  * stored in the residual's type (the activations' or fp32); x is formed from
  * the unrounded r'.  sb is the row distance of each tensor.  The backward call
- * recomputes what it needs from the forward's inputs. */
+ * recomputes what it needs from the forward's inputs.  Workspace with gradients:
+ * 12 channels bytes for each block (at most 10 an SM). */
 typedef struct seq_norm_plan_s *seq_norm_plan_t;
 
 typedef struct {
@@ -205,6 +222,7 @@ dgrad_status_t seq_norm_plan(long long rows, long long channels, seq_dtype_t dty
                              seq_act_t gate_act, float eps, seq_norm_plan_t *plan_out);
 dgrad_status_t seq_norm_run(seq_norm_plan_t plan, const seq_norm_args_t *args, void *stream);
 dgrad_status_t seq_norm_backward(seq_norm_plan_t plan, const seq_norm_grad_args_t *args, void *stream);
+size_t seq_norm_workspace_bytes(seq_norm_plan_t plan, int gradients);
 void seq_norm_destroy(seq_norm_plan_t plan);
 
 #ifdef __cplusplus
