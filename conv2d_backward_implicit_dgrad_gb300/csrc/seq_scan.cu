@@ -33,7 +33,10 @@ long long round_up(long long v, long long to) { return (v + to - 1) / to * to; }
 // Into how many spans to cut `length` tokens, walked by `blocks` blocks each
 // of which `resident` run at once: the cut whose last block ends first.  A
 // span costs its tokens and about 24 more for its start; cutting at all costs
-// `pass` of the main kernel's time for the pass over the chunks.
+// `pass` of the main kernel's time for the pass over the chunks (of measured
+// kernels: 197 of 286 us forwards, 119 of 600 backwards, at 16 states).  The 24
+// and the 2 % that a finer cut has to gain are estimates, held against a few
+// sizes and not swept.
 int spans_of(long long blocks, long long length, long long resident, double pass) {
     const long long most = std::max<long long>(1, std::min<long long>(kMostChunks, length / kLeastSpan));
     int best = 1;

@@ -11,7 +11,9 @@
 // What bounds it: a token of 64 channels and 16 states is 193 instructions of
 // a warp (112 of them the states' own: 64 packed multiply-adds of 2 cycles, 32
 // ex2 of 4, 16 loads from shared memory; the rest delta, gate, loads and the
-// store), with 16 warps an SM issued in 58 % of the cycles.  For 16384 tokens
+// store), with 16 warps an SM issued in 58 % of the cycles: the latency of
+// instructions that need one another, not the issue rate or memory, is what more
+// warps would hide.  For 16384 tokens
 // x 4096 channels in bf16 the main pass takes 286 us and the chunks' pass 197;
 // its 8 bytes a token and channel would take 79 us.  Measured and not kept:
 // steps of 8 tokens (that prompt 485 -> 489 us, ragged prompts 154 -> 196),
@@ -23,7 +25,9 @@
 // state it leaves from 0.  scan_state_kernel finds S and e of all chunks,
 // scan_join_kernel puts them together one after the other, and the main
 // kernel runs over all chunks with the states they are handed.  The exps are
-// then computed twice; nothing is approximated.
+// then computed twice; nothing is approximated.  (What a row's last chunk leaves
+// is not needed, nor, for the gradients, what those of its first span do; they
+// are worked on like the others.)
 #include <algorithm>
 #include <climits>
 #include <new>

@@ -45,9 +45,9 @@
  * is never read, outputs and gradients there are 0, and states stop at the
  * last token (a row of length 0 hands its state on unchanged).
  *
- * An infinity or NaN within a row reaches what the formulas below give it to
- * and no other row, token before it, channel or group.  One exception: a state
- * of seq_scan that first turns infinite at a row's last token can make its
+ * An infinity or NaN within a row reaches what the formulas below give it to,
+ * in its row and channel (of B or C: group), and nothing else.  One exception: a
+ * state of seq_scan that first turns infinite at a row's last token can make its
  * channel's grad_A NaN, which the formula would leave finite.
  */
 #ifndef SEQ_GB300_H
