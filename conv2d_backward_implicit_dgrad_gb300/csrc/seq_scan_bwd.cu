@@ -367,9 +367,14 @@ __global__ void __launch_bounds__(BwdShape<T, LN, WIDE>::THREADS, BwdShape<T, LN
                 }
             }
         };
-        // backwards, tokens 2 k + 1 and 2 k together
-#pragma unroll 1
-        for (int k = kSeg / 2 - 1; k >= 0; --k) {
+        // backwards, tokens 2 k + 1 and 2 k together, from the row's last token on
+        // (behind it the state and its gradient stay).  HALF: 2 k is that token, and
+        // the state after it, which may be infinite, is no term of grad_A.  (A copy of
+        // the body for it, chosen in the loop: 1013 -> 1015 us of a training step of
+        // 4 x 2048 tokens x 4096 channels; with that pair in front of the loop 1022,
+        // with a test in one body 1045.)
+        auto two_tokens = [&](auto half, int k) {
+            constexpr bool HALF = decltype(half)::value;
             const float *const fd = f_delta + 2 * k * CW + ch0, *const fu = f_u + 2 * k * CW + ch0;
             const float *const fy = f_dy + 2 * k * CW + ch0;
             const ulonglong2 qd0 = *reinterpret_cast<const ulonglong2 *>(fd);
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(BwdShape<T, LN, WIDE>::THREADS, BwdShape<T, LN
                     f2 ga = mul2(gn, a1);
                     f2 w = mul2(ga, h1);
                     sA1[c] = fma2(w, A2[c][n], sA1[c]);
-                    dA[c][n] = fma2(w, d1[c], dA[c][n]);
+                    if constexpr (!HALF) dA[c][n] = fma2(w, d1[c], dA[c][n]);
                     gn = fma2(y0[c], c0n, ga);
                     sB0[c] = fma2(gn, b0, sB0[c]);
                     dB0 = fma2(gn, x0[c], dB0);
@@ -428,6 +433,12 @@ __global__ void __launch_bounds__(BwdShape<T, LN, WIDE>::THREADS, BwdShape<T, LN
             }
             finish(2 * k + 1, sB1, sA1, sY1, v1);
             finish(2 * k, sB0, sA0, sY0, v0);
+        };
+#pragma unroll 1
+        for (int k = kSeg / 2 - 1; k >= 0; --k) {
+            if (at + 2 * k >= t1) continue;
+            if (at + 2 * k + 1 < t1) two_tokens(std::false_type(), k);
+            else two_tokens(std::true_type(), k);
         }
         // the results of the warp's channels
         __syncwarp();

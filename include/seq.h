@@ -46,9 +46,7 @@
  * last token (a row of length 0 hands its state on unchanged).
  *
  * An infinity or NaN within a row reaches what the formulas below give it to,
- * in its row and channel (of B or C: group), and nothing else.  One exception: a
- * state of seq_scan that first turns infinite at a row's last token can make its
- * channel's grad_A NaN, which the formula would leave finite.
+ * in its row and channel (of B or C: group), and nothing else.
  */
 #ifndef SEQ_GB300_H
 #define SEQ_GB300_H

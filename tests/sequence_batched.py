@@ -108,7 +108,7 @@ def scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, lens=None, state=None, go
         dy = gs[:, s] if z is None else gs[:, s] * gate[:, s]
         if z is not None:
             zs = torch.where(on[:, s], z[:, s], zero)
-            gr["z"][:, s] = gs[:, s] * (dsilu_size(zs) if magnitude else dsilu(zs)) * ys[s]
+            gr["z"][:, s] = torch.where(on[:, s], gs[:, s] * (dsilu_size(zs) if magnitude else dsilu(zs)) * ys[s], zero)
         gt = dy[..., None] * Ct + back
         per = (gt * Bt).sum(-1)
         through = gt * a * hs[s]

@@ -150,6 +150,36 @@ def test_scan_not_a_number_reaches_what_depends_on_it(t, what):
         same_places(getattr(g, name), want[2][name], mag[2][name], 2 * c + d + b * t, "grad " + name)
 
 
+@pytest.mark.parametrize("what", ["u", "B"])
+@pytest.mark.parametrize("has_z", [True, False])
+@pytest.mark.parametrize("length", [24, 25, 26, 31, 413])
+def test_scan_infinite_state_after_the_last_token(length, has_z, what):
+    """An infinity that the last token brings in is in no state before a token: grad_A keeps to what it was."""
+    gen = torch.Generator().manual_seed(66)
+    b, t, d, n, lens = 2, length + 5, 12, 5, [length, length + 5]
+    v = dict(u=rand(gen, b, t, d), dt=rand(gen, b, t, d), B=rand(gen, b, t, 1, n), C=rand(gen, b, t, 1, n),
+             z=rand(gen, b, t, d) if has_z else None)
+    go = rand(gen, b, t, d)
+    p = dict(A=-rand(gen, d, n).abs() - 0.05, D=rand(gen, d), dt_bias=rand(gen, d) - 2.0, state=rand(gen, b, d, n))
+    v[what][0, length - 1, 0, 0 if what == "B" else ...] = float("inf")
+    want = ref.scan(**v, **p, lens=lens, go=go)
+    mag = ref.scan(**v, **p, lens=lens, go=go, magnitude=True)
+    n_t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    with dg.ScanPlan(b, t, d, n, dtype="fp32") as plan:
+        ck, final = plan.checkpoints(), torch.empty(b, d, n, device="cuda")
+        names = dict(D=p["D"], z=v["z"], dt_bias=p["dt_bias"], state=p["state"], lengths=n_t)
+        first = (v["u"], v["dt"], p["A"], v["B"], v["C"])
+        out = plan.run(*first, checkpoints=ck, final_state=final, **names)
+        g = plan.backward(go, *first, ck, **names)
+    assert bool(torch.isfinite(want[2]["A"]).all())
+    c = 64 + 4 * t + n
+    same_places(out, want[0], mag[0], c, "out")
+    same_places(final, want[1], mag[1], c, "final")
+    for name in ("u", "dt", "B", "C", "z", "A", "D", "dt_bias", "state"):
+        if getattr(g, name) is not None:
+            same_places(getattr(g, name), want[2][name], mag[2][name], 2 * c + d + b * t, "grad " + name)
+
+
 @pytest.mark.parametrize("d", [64, 37, 2051])
 def test_norm_keeps_to_its_row(d):
     gen = torch.Generator().manual_seed(65)
